@@ -329,9 +329,7 @@ def run(s):
     if case["op"] == "append":
         kvq.latent_append(g, LAYER, s["pool"], s["table"], s["start"], s["n"], s["off"], max(s["lens"]), s["lat"],
                           s["rope"], s["status"])
-        if "held" not in s:   # views for the comparison, no part of the call
-            s["held"] = _held(s)
-        return s["held"]
+        return _held(s)
     if case["op"] == "read":
         kvq.latent_read(g, LAYER, s["pool"], s["table"], s["start"], s["n"], s["off"], max(s["lens"]), s["lat"],
                         s["rope"], s["status"])
