@@ -682,12 +682,12 @@ __global__ void __launch_bounds__(LaCfg<FMT, N>::THREADS, 1) latent_attn_tc(Late
         if (lane == 0) *reinterpret_cast<volatile int*>(smem + C::SM_PROG) = j + 1;
       }
     }
-    if (timed_out) {   // copies in flight must land before the CTA ends: the lane's last few
-      *abort_flag = 1;
-      for (uint32_t i = issued > 3 ? issued - 3 : 0; i < issued; i++)
-        mbar_wait(BAR(C::B_FULL + i % 3 + (lane == 2 || lane == 3 ? 3 : 0)), (i / 3) & 1);
-      __syncwarp();
-    }
+    // Copies in flight must land before the CTA ends, also where another role gave up after the last one was issued: the
+    // lane's last few.  (None of these phases can be two behind: the next one lacks this lane's arrival.)
+    if (timed_out) *abort_flag = 1;
+    for (uint32_t i = issued > 3 ? issued - 3 : 0; i < issued; i++)
+      mbar_wait(BAR(C::B_FULL + i % 3 + (lane == 2 || lane == 3 ? 3 : 0)), (i / 3) & 1);
+    __syncwarp();
   } else if (warp < 8) {
     // ================================================================= queries
     int part = 0, done = 0;

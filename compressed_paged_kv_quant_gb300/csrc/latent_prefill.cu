@@ -432,11 +432,10 @@ __global__ void __launch_bounds__(LP_THREADS, 1) latent_prefill_tc(LatentPrefill
     // ================================================================= copies
     if (lane == 0) {
       while (u < 5 * n && !timed_out) copy_unit();
-      if (timed_out) {   // copies in flight must land before the CTA ends
-        *abort_flag = 1;
-        mbar_wait(BAR(LPB_Q), 0);
-        for (int i = max(0, u - LP_RING); i < u; i++) mbar_wait(BAR(LPB_FULL + i % LP_RING), (i / LP_RING) & 1);
-      }
+      // copies in flight must land before the CTA ends, also where another role gave up after the last one was issued
+      if (timed_out) *abort_flag = 1;
+      mbar_wait(BAR(LPB_Q), 0);
+      for (int i = max(0, u - LP_RING); i < u; i++) mbar_wait(BAR(LPB_FULL + i % LP_RING), (i / LP_RING) & 1);
     }
     timed_out = __shfl_sync(0xFFFFFFFFu, timed_out, 0);
   }
