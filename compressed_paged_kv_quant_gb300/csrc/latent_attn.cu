@@ -640,9 +640,9 @@ __global__ void __launch_bounds__(LaCfg<FMT, N>::THREADS, 1) latent_attn_tc(Late
     if (!ok) {
       timed_out = true;
       *abort_flag = 1;
-      t5_commit_if(one, BAR(C::B_END));   // every MMA issued must be complete before the tensor memory goes
-      mbar_wait(BAR(C::B_END), 0);
     }
+    t5_commit_if(one, BAR(C::B_END));   // every MMA issued must be complete before the tensor memory goes, also where
+    mbar_wait(BAR(C::B_END), 0);        // the softmax gave up on them
     __syncwarp();
   } else if (warp == 5) {
     // ================================================================= bulk copies

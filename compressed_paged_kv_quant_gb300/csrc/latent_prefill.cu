@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(LP_THREADS, 1) latent_prefill_tc(LatentPrefill
     if (!ok) {
       timed_out = true;
       *abort_flag = 1;
-      t5_commit_if(one, BAR(LPB_END));   // every MMA issued must be complete before the tensor memory goes
-      mbar_wait(BAR(LPB_END), 0);
     }
+    t5_commit_if(one, BAR(LPB_END));   // every MMA issued must be complete before the tensor memory goes, also where
+    mbar_wait(BAR(LPB_END), 0);        // the softmax gave up on them
     __syncwarp();
   } else {
     // ================================================================= copies

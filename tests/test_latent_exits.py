@@ -42,3 +42,10 @@ def test_copies_land_before_the_cta_ends(name, wait):
     """A copy role that has issued its last copies leaves its loop in good order while they are under way; another role
     may give up on them."""
     assert unconditional(source(name), wait)
+
+
+@pytest.mark.parametrize("name,wait", [("latent_attn.cu", r"mbar_wait\(BAR\(C::B_END\), 0\);"),
+                                       ("latent_prefill.cu", r"mbar_wait\(BAR\(LPB_END\), 0\);")])
+def test_mmas_complete_before_the_cta_ends(name, wait):
+    """The issuing warp may have issued its last products in good order when the softmax gives up on them."""
+    assert unconditional(source(name), wait)
