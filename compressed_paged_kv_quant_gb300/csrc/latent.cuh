@@ -146,6 +146,7 @@ int latent_launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaSt
 int launch_latent_append(int fmt, const LatentTokenArgs& a, cudaStream_t stream);
 int launch_latent_read(int fmt, const LatentTokenArgs& a, cudaStream_t stream);
 int launch_latent_attn(int fmt, const LatentAttnArgs& a, cudaStream_t stream);
+size_t latent_attn_needs(int heads, int lanes, int max_n_q, int max_seq_len);
 size_t latent_attn_workspace(int heads, int lanes, int max_n_q, int max_seq_len);
 int launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t stream);
 size_t latent_prefill_workspace(int lanes, int heads, int n_q_rows, int max_n_q, int max_n_k);

@@ -25,8 +25,8 @@
 //
 // Work: the (lane, page) list is cut into W equal ranges, one CTA a range and row tile, so ragged
 // lanes balance; a lane within one range is finished there, else its parts are FP32 partials that
-// latent_attn_combine merges.  A part's slot is range + lane: along the list each part moves one of
-// the two up, so no two parts share a slot and W + lanes slots are enough.
+// latent_attn_combine merges.  A range holds two parts at most that are not a whole lane: the rest of a lane that began
+// before it, and the first pages of one that goes on behind it.  The former takes slot w of 2 W, the latter W + w.
 // The kernels are launched programmatically: a start overlaps the end of the kernel before it.
 // Every wait is bounded; on a timeout the CTA flags KVQ_STATUS_TIMEOUT and ends.
 //
@@ -118,21 +118,29 @@ static LaGrid la_grid(int heads, int max_n_q, int max_seq_len) {
   const int N = la_rows(heads, max_n_q);
   LaGrid g;
   g.T = (int)(((int64_t)heads * max_n_q + N - 1) / N);
-  const bool ranges = g.T > 0 && g.T <= LA_MAX_T && (max_seq_len + P - 1) / P > LA_LANE_TILES;
+  const bool ranges = g.T > 0 && g.T <= LA_MAX_T && max_seq_len > LA_LANE_TILES * P;
   g.W = ranges ? LA_SMS / g.T : 0;
   return g;
 }
 
-size_t latent_attn_workspace(int heads, int lanes, int max_n_q, int max_seq_len) {
+static size_t la_bytes(int64_t rows, int lanes) {   // rows of partials
+  return (size_t)rows * (LAT + 2) * sizeof(float) + ((size_t)lanes + 1) * sizeof(int) + 256;
+}
+
+// Bytes that this very call touches, and a bound of them for it and every smaller one (W T is at most the SMs, for any T).
+size_t latent_attn_needs(int heads, int lanes, int max_n_q, int max_seq_len) {
   const LaGrid g = la_grid(heads, max_n_q, max_seq_len);
-  if (g.W == 0) return 256;
-  return ((size_t)g.W + lanes) * g.T * la_rows(heads, max_n_q) * (LAT + 2) * sizeof(float) +
-         ((size_t)lanes + 1) * sizeof(int) + 256;
+  return g.W == 0 ? 256 : la_bytes((int64_t)2 * g.W * g.T * la_rows(heads, max_n_q), lanes);
+}
+
+size_t latent_attn_workspace(int heads, int lanes, int max_n_q, int max_seq_len) {
+  const bool ranges = max_n_q > 0 && max_seq_len > LA_LANE_TILES * P;
+  return ranges ? la_bytes((int64_t)2 * LA_SMS * la_rows(heads, max_n_q), lanes) : 256;
 }
 
 // After the partials: pages of a range, then for each lane the pages of the list before it.
 __device__ __forceinline__ int* la_meta(const LatentAttnArgs& a, const LaGrid& g, int N) {
-  return reinterpret_cast<int*>(a.ws + (int64_t)(g.W + a.c.lanes) * g.T * N * (LAT + 2));
+  return reinterpret_cast<int*>(a.ws + (int64_t)2 * g.W * g.T * N * (LAT + 2));
 }
 
 // pages of lane b in the list
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(LaCfg<FMT, N>::THREADS, 1) latent_attn_tc(Late
       }
       sync4();
       const bool whole = p.t0 == 0 && p.t1 == p.tiles;
-      const int64_t slot = ((int64_t)(w + p.b) * g.T + rt);
+      const int64_t slot = (int64_t)(w + (p.t0 == 0 ? g.W : 0)) * g.T + rt;
       if (whole) {
         if (tid < N) {
           const int r = tid;
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(LaCfg<FMT, N>::THREADS, 1) latent_attn_tc(Late
           fac[r] = s > 0.f ? 1.0f / s : 0.f;
         }
       } else if (quad == 0 && lane < 4) {
-        float2* ml = reinterpret_cast<float2*>(a.ws + (int64_t)(g.W + a.c.lanes) * g.T * N * LAT) + slot * N;
+        float2* ml = reinterpret_cast<float2*>(a.ws + (int64_t)2 * g.W * g.T * N * LAT) + slot * N;
 #pragma unroll
         for (int i = 0; i < 2 * J; i++) {
           const int r = 8 * (i >> 1) + c0 + (i & 1);
@@ -886,8 +894,8 @@ __global__ void __launch_bounds__(LC_THREADS, Z == 1 ? 3 : 2) latent_attn_combin
   const int tiles = (pos0 + min(nq - 1, (r0 + N - 1) / a.heads) + P) / P;
   const int parts = (at + tiles - 1) / R - first + 1;
   if (parts < 2) return;                                              // finished by its only part
-  const int64_t slot0 = first + b;
-  const float2* ml = reinterpret_cast<const float2*>(a.ws + (int64_t)(g.W + a.c.lanes) * g.T * N * LAT);
+  auto slot = [&](int s) { return (int64_t)((s == 0 ? g.W : s) + first); };   // of the lane's part s
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + (int64_t)2 * g.W * g.T * N * LAT);
   static_assert(Z == 1 || Z == 2, "a lane's share of a row is 4 float4 or 2");
   constexpr int WARPS = LC_THREADS / 32, PER = (LA_SMS + 31) / 32;   // parts a lane of the warp weighs
   const int64_t step = (int64_t)g.T * N * LAT / 4;                   // from a part to the next, in float4
@@ -896,13 +904,13 @@ __global__ void __launch_bounds__(LC_THREADS, Z == 1 ? 3 : 2) latent_attn_combin
   for (int rb = alone ? r_first * WARPS : r_first; rb < N && r0 + rb < rows; rb += alone ? r_step * WARPS : r_step) {
     const int r = alone ? rb + warp : rb;
     if (r >= N || r0 + r >= rows) break;               // (alone: no barrier follows)
-    const float4* src = reinterpret_cast<const float4*>(a.ws + ((slot0 * g.T + rt) * N + r) * LAT) + z * D + lane;
+    const float4* src = reinterpret_cast<const float4*>(a.ws + ((int64_t)rt * N + r) * LAT) + z * D + lane;
     float2 e[PER];
     float mx = -INFINITY;
 #pragma unroll
     for (int k = 0; k < PER; k++) {
       const int s = 32 * k + lane;
-      e[k] = s < parts ? ml[((slot0 + s) * g.T + rt) * N + r] : make_float2(-INFINITY, 0.f);
+      e[k] = s < parts ? ml[(slot(s) * g.T + rt) * N + r] : make_float2(-INFINITY, 0.f);
       mx = fmaxf(mx, e[k].x);
     }
 #pragma unroll
@@ -928,7 +936,7 @@ __global__ void __launch_bounds__(LC_THREADS, Z == 1 ? 3 : 2) latent_attn_combin
         for (int i = 0; i < B; i++) {
           const int s = warp + WARPS * (half * B + i);
 #pragma unroll
-          for (int q = 0; q < Q; q++) o[i][q] = s < parts ? src[s * step + 32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int q = 0; q < Q; q++) o[i][q] = s < parts ? src[slot(s) * step + 32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < B; i++) {
@@ -950,7 +958,7 @@ __global__ void __launch_bounds__(LC_THREADS, Z == 1 ? 3 : 2) latent_attn_combin
         const float f = __shfl_sync(0xFFFFFFFFu, e[k].x, i);
 #pragma unroll
         for (int q = 0; q < Q; q++) {
-          const float4 o = src[(32 * k + i) * step + 32 * q];
+          const float4 o = src[slot(32 * k + i) * step + 32 * q];
           sum[q].x = fmaf(o.x, f, sum[q].x);
           sum[q].y = fmaf(o.y, f, sum[q].y);
           sum[q].z = fmaf(o.z, f, sum[q].z);

@@ -362,7 +362,7 @@ int kvq_paged_latent_attn(const kvq_latent_geom* g, int layer, const void* pool,
       (rc = check_out_rows(out, n_q_rows, g->num_q_heads)))
     return rc;
   if (!aligned16(pool) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  if (ws_bytes < latent_attn_workspace(g->num_q_heads, lanes, max_n_q, max_seq_len)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < latent_attn_needs(g->num_q_heads, lanes, max_n_q, max_seq_len)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   LatentAttnArgs a{};
   a.c = latent_view(g, layer, pool, pool_bytes, page_table, max_pages, lanes, d_status);
   a.q_pos0 = q_pos0;

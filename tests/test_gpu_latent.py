@@ -835,3 +835,20 @@ def test_expanded_two_splits_of_many_rows(kvq, heads, nqs, prefix):
     c.call()
     assert c.status.item() == 0
     c.check()
+
+
+@FORMATS
+@pytest.mark.parametrize("heads", [16, 128])
+def test_one_workspace_for_all_calls_of_a_server(kvq, fmt, heads):
+    """A workspace sized for the largest call (chunks of up to 64 queries, 16 lanes, 8,192 tokens) serves single
+    tokens, drafted tokens and chunks, and nothing behind it is touched."""
+    size = kvq.latent_workspace_bytes(kvq.latent_geom(fmt, 2, heads), 16, 64, 8192)
+    whole = torch.full((size + 65536,), 0xEE, dtype=torch.uint8, device="cuda")
+    for lens, nqs in (([8192, 100], [1, 1]), ([3000, 2000, 700], [4, 1, 2]), ([1500, 700], [30, 1]), ([900, 300], [64, 1]),
+                      ([700 + 13 * i for i in range(16)], [1] * 16)):
+        c = Absorbed(kvq, fmt, heads, lens, nqs, 240 + heads, head_first=False)
+        c.ws = whole[:size]
+        c.call()
+        assert c.status.item() == 0
+        c.check()
+    assert bool((whole[size:] == 0xEE).all())

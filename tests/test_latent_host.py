@@ -189,3 +189,18 @@ def test_sizes_past_32_bits_are_refused(L):
     assert _attn(L, g, lanes=big, max_pages=1 << 20, max_seq=1 << 26, ws_bytes=(1 << 62)) == kvq.ERR_UNSUPPORTED
     assert _append(L, g, lanes=big, most=big) == kvq.ERR_UNSUPPORTED
     assert _append(L, g, "kvq_latent_read", lanes=big, most=big) == kvq.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("heads", [1, 16, 24, 100, 128])
+def test_workspace_for_the_most_serves_every_smaller_call(L, heads):
+    """A server sizes one workspace for its largest call and makes all of its calls with it."""
+    g = kvq.latent_geom(kvq.LATENT_BF16, 2, heads)
+    lanes, most, long = (1, 7, 64, 300), (0, 1, 2, 3, 16, 38, 39, 64, 512), (0, 64, 512, 513, 5000, 40960, 2 ** 31 - 1)
+    for i, b in enumerate(lanes):
+        for j, n in enumerate(most):
+            for k, m in enumerate(long):
+                size = kvq.latent_workspace_bytes(g, b, n, m)
+                assert size > 0
+                for less in ((lanes[i - 1], n, m) if i else None, (b, most[j - 1], m) if j else None,
+                             (b, n, long[k - 1]) if k else None):
+                    assert less is None or kvq.latent_workspace_bytes(g, *less) <= size, (b, n, m, less)
