@@ -149,6 +149,7 @@ int launch_latent_attn(int fmt, const LatentAttnArgs& a, cudaStream_t stream);
 size_t latent_attn_needs(int heads, int lanes, int max_n_q, int max_seq_len);
 size_t latent_attn_workspace(int heads, int lanes, int max_n_q, int max_seq_len);
 int launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t stream);
-size_t latent_prefill_workspace(int lanes, int heads, int n_q_rows, int max_n_q, int max_n_k);
+size_t latent_prefill_needs(int lanes, int heads, int max_n_q, int max_n_k);
+size_t latent_prefill_workspace(int lanes, int heads, int max_n_q, int max_n_k);
 
 }  // namespace kvq

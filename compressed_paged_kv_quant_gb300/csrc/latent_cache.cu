@@ -323,7 +323,7 @@ size_t kvq_latent_workspace_bytes(const kvq_latent_geom* g, int lanes, int max_n
 size_t kvq_latent_prefill_workspace_bytes(int lanes, int num_heads, int n_q_rows, int max_n_q, int max_n_k) {
   if (lanes < 0 || num_heads <= 0 || num_heads > LMAX_HEADS || n_q_rows < 0 || max_n_q < 0 || max_n_k < 0) return 0;
   if (max_n_q > LMAX_PREFILL || max_n_k > LMAX_PREFILL) return 0;
-  return latent_prefill_workspace(lanes, num_heads, n_q_rows, max_n_q, max_n_k);
+  return latent_prefill_workspace(lanes, num_heads, max_n_q, max_n_k);
 }
 
 int kvq_latent_append(const kvq_latent_geom* g, int layer, void* pool, size_t pool_bytes, const int32_t* page_table,
@@ -401,8 +401,7 @@ int kvq_latent_prefill_attn(int num_heads, int lanes, const int32_t* q_pos0, con
       !mappable(k_nope, n_k_rows, num_heads) || !mappable(k_rope, n_k_rows, 1) || !mappable(v, n_k_rows, num_heads))
     return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  if (ws_bytes < latent_prefill_workspace(lanes, num_heads, n_q_rows, max_n_q, max_n_k))
-    return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < latent_prefill_needs(lanes, num_heads, max_n_q, max_n_k)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   LatentPrefillArgs a{};
   a.q_pos0 = q_pos0;
   a.n_q = n_q;

@@ -118,9 +118,24 @@ static LpSplit lp_split(int lanes, int heads, int max_n_q, int max_n_k) {
   return s;
 }
 
-size_t latent_prefill_workspace(int lanes, int heads, int n_q_rows, int max_n_q, int max_n_k) {
+// Partials lie by (lane, query, head, split), so that their bytes follow from the arguments that decide the split.
+__host__ __device__ static int64_t lp_partials(const LatentPrefillArgs& a) { return (int64_t)a.lanes * a.max_n_q * a.heads; }   // of a split
+static size_t lp_bytes(int64_t partials) { return (size_t)partials * (VDIM + 2) * sizeof(float) + 256; }
+
+// Bytes that this very call touches, and a bound of them for it and every smaller one.  No fewer than
+// 2 LP_SPLIT_TILES key tiles are split (LP_TAIL_TILES are more than half of such), into LP_SPLIT_TILES each at least; and
+// splits x CTAs are at most the SMs, or 2 for each of fewer CTAs than SMs, of LP_ROWS rows each.
+size_t latent_prefill_needs(int lanes, int heads, int max_n_q, int max_n_k) {
   const LpSplit s = lp_split(lanes, heads, max_n_q, max_n_k);
-  return s.splits == 1 ? 256 : (size_t)n_q_rows * heads * s.splits * (VDIM + 2) * sizeof(float) + 256;
+  return s.splits == 1 ? 256 : lp_bytes((int64_t)lanes * max_n_q * heads * s.splits);
+}
+
+size_t latent_prefill_workspace(int lanes, int heads, int max_n_q, int max_n_k) {
+  const int tiles = (max_n_k + LP_KEYS - 1) / LP_KEYS;
+  static_assert(2 * LP_TAIL_TILES >= 2 * LP_SPLIT_TILES, "tails only of as many tiles");
+  if (tiles < 2 * LP_SPLIT_TILES) return 256;
+  const int64_t most = (int64_t)2 * LP_SMS * LP_ROWS, splits = std::min(LP_SMS, (tiles + LP_SPLIT_TILES - 1) / LP_SPLIT_TILES);
+  return lp_bytes(std::min(most, std::min(most, (int64_t)heads * max_n_q) * std::min<int64_t>(most, lanes) * splits));
 }
 
 // grid: (row tiles x heads, lanes, splits)
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) latent_prefill_tc(LatentPrefill
       const int w0 = q0 + 128 * x + 32 * (warp & 3);          // the warp's first row
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const bool whole = sp.splits == 1;
-      const int64_t part = ((int64_t)(row0 + qi) * a.heads + h) * sp.splits + s;
+      const int64_t part = (((int64_t)b * a.max_n_q + qi) * a.heads + h) * sp.splits + s;
       auto out_rows = [&](int c, const uint32_t (&v)[32], uint8_t* base, int64_t row_bytes) {
         const uint32_t mine = sm + LP_SM_Q + (c & 1) * (LP_ROWS * 128) + (128 * x + 32 * (warp & 3)) * 128;
 #pragma unroll
@@ -340,7 +355,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) latent_prefill_tc(LatentPrefill
         }
       } else {
         const int64_t per_row = (int64_t)a.heads * sp.splits;   // parts from a row to the next
-        uint8_t* base = reinterpret_cast<uint8_t*>(a.ws + (((int64_t)(row0 + w0) * a.heads + h) * sp.splits + s) * VDIM);
+        uint8_t* base = reinterpret_cast<uint8_t*>(a.ws + ((((int64_t)b * a.max_n_q + w0) * a.heads + h) * sp.splits + s) * VDIM);
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
           uint32_t o[32];
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) latent_prefill_tc(LatentPrefill
           out_rows(c, o, base + 128 * c, per_row * VDIM * 4);
         }
         if (live)
-          reinterpret_cast<float2*>(a.ws + (int64_t)a.n_q_rows * a.heads * sp.splits * VDIM)[part] = make_float2(m, l);
+          reinterpret_cast<float2*>(a.ws + lp_partials(a) * sp.splits * VDIM)[part] = make_float2(m, l);
       }
     }
   } else if (warp == 8) {
@@ -460,8 +475,8 @@ __global__ void __launch_bounds__(256) latent_prefill_combine(LatentPrefillArgs 
   const int qi = (int)(item / a.heads), h = (int)(item % a.heads), lane = threadIdx.x & 31;
   if (!ok || qi >= nq) return;
   const int parts = (pos0 + qi) / LP_KEYS / sp.tiles + 1;
-  const int64_t part = ((int64_t)(row0 + qi) * a.heads + h) * sp.splits;
-  const float2* ml = reinterpret_cast<const float2*>(a.ws + (int64_t)a.n_q_rows * a.heads * sp.splits * VDIM) + part;
+  const int64_t part = (((int64_t)blockIdx.y * a.max_n_q + qi) * a.heads + h) * sp.splits;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + lp_partials(a) * sp.splits * VDIM) + part;
   const float4* o = reinterpret_cast<const float4*>(a.ws + part * VDIM) + lane;
   float mx = -INFINITY, den = 0.f;
   for (int s = 0; s < parts; s++) mx = fmaxf(mx, ml[s].x);
@@ -492,12 +507,12 @@ __global__ void __launch_bounds__(256) latent_prefill_combine2(LatentPrefillArgs
   const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * LP_PAIRS, items = (int64_t)nq * a.heads;
   const int lane = threadIdx.x & 31;
   const float4* o = reinterpret_cast<const float4*>(a.ws) + lane;
-  const float4* ml = reinterpret_cast<const float4*>(a.ws + (int64_t)a.n_q_rows * a.heads * 2 * VDIM);   // (m, l) of both
+  const float4* ml = reinterpret_cast<const float4*>(a.ws + lp_partials(a) * 2 * VDIM);   // (m, l) of both
   float4 e[LP_PAIRS], v[LP_PAIRS][2];
 #pragma unroll
   for (int k = 0; k < LP_PAIRS; k++) {
     if (first + k >= items) break;
-    const int64_t at = (int64_t)row0 * a.heads + first + k;
+    const int64_t at = (int64_t)blockIdx.y * a.max_n_q * a.heads + first + k;
     const bool two = pos0 + (int)((first + k) / a.heads) >= LP_KEYS * sp.tiles;   // does the row reach the second split?
     e[k] = ml[at];
     v[k][0] = o[at * (2 * VDIM / 4)];

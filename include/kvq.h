@@ -347,7 +347,8 @@ size_t kvq_latent_token_bytes(const kvq_latent_geom* geom);
  * tokens, and of every call with fewer of any of them (at most 40 MB, and 4 bytes a lane); 0 on a bad geom or bad sizes
  * (negative, or num_q_heads * max_n_q above 2^31 - 1).  (Never 0 otherwise.) */
 size_t kvq_latent_workspace_bytes(const kvq_latent_geom* geom, int lanes, int max_n_q, int max_seq_len);
-/* Workspace of kvq_latent_prefill_attn; 0 on bad sizes (negative, more than 128 heads, or max_n_q or max_n_k
+/* Workspace of kvq_latent_prefill_attn for a call of these sizes and every one with fewer lanes, heads, queries or keys
+ * (at most 40.5 MB; whatever n_q_rows is); 0 on bad sizes (negative, more than 128 heads, or max_n_q or max_n_k
  * above 2^31 - 257). */
 size_t kvq_latent_prefill_workspace_bytes(int lanes, int num_heads, int n_q_rows, int max_n_q, int max_n_k);
 

@@ -852,3 +852,33 @@ def test_one_workspace_for_all_calls_of_a_server(kvq, fmt, heads):
         assert c.status.item() == 0
         c.check()
     assert bool((whole[size:] == 0xEE).all())
+
+
+def test_one_workspace_for_all_expanded_calls_of_a_server(kvq):
+    """A workspace sized for the largest call (8 lanes, 32 heads, chunks of 2,048 over 16,000 keys) serves every smaller
+    one, also from rows in the middle of large buffers, and nothing behind it is touched."""
+    size = kvq.latent_prefill_workspace_bytes(8, 32, 16384, 2048, 16000)
+    whole = torch.full((size + 65536,), 0xEE, dtype=torch.uint8, device="cuda")
+    for heads, nqs, prefix, gap in ((32, [256], [3000], 1), (20, [1024], [4500], 3), (16, [40, 1], [2500, 2100], 3000),
+                                    (4, [300, 7, 256], [2000, 2300, 0], 700), (2, [130] * 8, [2100] * 8, 1), (32, [2048], [0], 1)):
+        c = Expanded(kvq, heads, nqs, prefix, 250 + heads, gap=gap)
+        c.ws = whole[:size]
+        c.call()
+        assert c.status.item() == 0
+        c.check()
+    assert bool((whole[size:] == 0xEE).all())
+
+
+@pytest.mark.parametrize("heads,nqs,prefix", [(2, [40, 300], [6000, 3000]), (20, [260, 3], [6000, 100]), (1, [9, 257], [2500, 2000])])
+def test_expanded_parts_stay_in_their_workspace(kvq, heads, nqs, prefix):
+    """The bytes that this very call needs, with a guard behind them."""
+    c = Expanded(kvq, heads, nqs, prefix, 260 + heads, gap=900)
+    tiles, ctas = -(-c.most_k // 128), len(nqs) * heads * -(-c.most // 256)
+    splits = 2 if 2 * ctas > 152 else -(-tiles // max(8, -(-tiles // (152 // ctas))))
+    size = len(nqs) * c.most * heads * splits * 130 * 4 + 256
+    assert size <= c.ws.numel()
+    whole = torch.full((size + 65536,), 0xEE, dtype=torch.uint8, device="cuda")
+    c.ws = whole[:size]
+    c.call()
+    assert c.status.item() == 0 and bool((whole[size:] == 0xEE).all())
+    c.check()

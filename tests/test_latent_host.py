@@ -204,3 +204,23 @@ def test_workspace_for_the_most_serves_every_smaller_call(L, heads):
                 for less in ((lanes[i - 1], n, m) if i else None, (b, most[j - 1], m) if j else None,
                              (b, n, long[k - 1]) if k else None):
                     assert less is None or kvq.latent_workspace_bytes(g, *less) <= size, (b, n, m, less)
+
+
+def test_prefill_workspace_for_the_most_serves_every_smaller_call(L):
+    """The same for the expanded form, whose split depends on lanes, heads, queries and keys."""
+    axes = [(1, 2, 8, 9, 300), (1, 16, 25, 32, 128), (1, 100, 256, 257, 1024, 2048, 2 ** 31 - 257),
+            (1, 1000, 1920, 1921, 5000, 16000, 65536, 2 ** 31 - 257)]
+    size = {}
+    for lanes in axes[0]:
+        for heads in axes[1]:
+            for n in axes[2]:
+                for m in axes[3]:
+                    size[lanes, heads, n, m] = kvq.latent_prefill_workspace_bytes(lanes, heads, 4096, n, m)
+    for at, here in size.items():
+        assert here > 0
+        for i, axis in enumerate(axes):
+            j = axis.index(at[i])
+            if j:
+                assert size[at[:i] + (axis[j - 1],) + at[i + 1:]] <= here, (at, i)
+    rows = {kvq.latent_prefill_workspace_bytes(2, 16, r, 256, 16000) for r in (1, 512, 4096, 2 ** 31 - 1)}
+    assert len(rows) == 1
