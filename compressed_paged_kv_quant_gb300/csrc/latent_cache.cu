@@ -227,16 +227,16 @@ int check_latent_geom(const kvq_latent_geom* g) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-// bf16 rows: present, aligned, strides whole 16 B units
-int check_rows(const kvq_rows* r) {
+// bf16 rows: present, aligned, the strides that are used whole 16 B units
+int check_rows(const kvq_rows* r, int rows, int heads) {
   if (!r || !r->ptr) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(r->ptr) || r->row_stride % 8 || r->head_stride % 8) return KVQ_ERR_ALIGNMENT;
+  if (!aligned16(r->ptr) || (rows > 1 && r->row_stride % 8) || (heads > 1 && r->head_stride % 8)) return KVQ_ERR_ALIGNMENT;
   return KVQ_OK;
 }
 
 // rows that are written: no two at one place
 int check_out_rows(const kvq_rows* r, int rows, int heads) {
-  const int rc = check_rows(r);
+  const int rc = check_rows(r, rows, heads);
   if (rc) return rc;
   return (rows > 1 && r->row_stride == 0) || (heads > 1 && r->head_stride == 0) ? KVQ_ERR_INVALID_ARG : KVQ_OK;
 }
@@ -248,8 +248,8 @@ bool mappable(const kvq_rows* r, int rows, int heads) {
          (heads <= 1 || (r->head_stride >= 0 && r->head_stride < end));
 }
 
-RowsView rows_view(const kvq_rows* r) {
-  return RowsView{static_cast<__nv_bfloat16*>(r->ptr), r->row_stride, r->head_stride};
+RowsView rows_view(const kvq_rows* r, int rows, int heads) {
+  return RowsView{static_cast<__nv_bfloat16*>(r->ptr), rows > 1 ? r->row_stride : 0, heads > 1 ? r->head_stride : 0};
 }
 
 size_t latent_page_bytes(const kvq_latent_geom* g) { return (size_t)g->num_layers * latent_block(g->format); }
@@ -287,8 +287,8 @@ int latent_tokens(bool append, const kvq_latent_geom* g, int layer, const void* 
   if (!pool || !page_table || !start_pos || !n_tok || !tok_offset || !d_status) return KVQ_ERR_INVALID_ARG;
   if (pool_bytes < latent_page_bytes(g)) return KVQ_ERR_INVALID_ARG;
   if (n_rows > 0) {
-    rc = append ? check_rows(latent) : check_out_rows(latent, n_rows, 1);
-    if (!rc) rc = append ? check_rows(rope) : check_out_rows(rope, n_rows, 1);
+    rc = append ? check_rows(latent, n_rows, 1) : check_out_rows(latent, n_rows, 1);
+    if (!rc) rc = append ? check_rows(rope, n_rows, 1) : check_out_rows(rope, n_rows, 1);
     if (rc) return rc;
   }
   if (!latent || !rope) return KVQ_ERR_INVALID_ARG;
@@ -300,8 +300,8 @@ int latent_tokens(bool append, const kvq_latent_geom* g, int layer, const void* 
   a.tok_offset = tok_offset;
   a.max_tok = max_tok;
   a.n_rows = n_rows;
-  a.latent = rows_view(latent);
-  a.rope = rows_view(rope);
+  a.latent = rows_view(latent, n_rows, 1);
+  a.rope = rows_view(rope, n_rows, 1);
   return append ? launch_latent_append(g->format, a, (cudaStream_t)stream)
                 : launch_latent_read(g->format, a, (cudaStream_t)stream);
 }
@@ -358,7 +358,7 @@ int kvq_paged_latent_attn(const kvq_latent_geom* g, int layer, const void* pool,
   if (!pool || !page_table || !q_pos0 || !n_q || !q_offset || !seq_len || !workspace || !d_status)
     return KVQ_ERR_INVALID_ARG;
   if (pool_bytes < latent_page_bytes(g)) return KVQ_ERR_INVALID_ARG;
-  if ((rc = check_rows(q_latent)) || (rc = check_rows(q_rope)) ||
+  if ((rc = check_rows(q_latent, n_q_rows, g->num_q_heads)) || (rc = check_rows(q_rope, n_q_rows, g->num_q_heads)) ||
       (rc = check_out_rows(out, n_q_rows, g->num_q_heads)))
     return rc;
   if (!aligned16(pool) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
@@ -373,9 +373,9 @@ int kvq_paged_latent_attn(const kvq_latent_geom* g, int layer, const void* pool,
   a.n_q_rows = n_q_rows;
   a.max_seq_len = max_seq_len;
   a.heads = g->num_q_heads;
-  a.ql = rows_view(q_latent);
-  a.qr = rows_view(q_rope);
-  a.out = rows_view(out);
+  a.ql = rows_view(q_latent, n_q_rows, a.heads);
+  a.qr = rows_view(q_rope, n_q_rows, a.heads);
+  a.out = rows_view(out, n_q_rows, a.heads);
   a.scale_log2 = sm_scale * LOG2E;
   a.ws = static_cast<float*>(workspace);
   return launch_latent_attn(g->format, a, (cudaStream_t)stream);
@@ -394,9 +394,13 @@ int kvq_latent_prefill_attn(int num_heads, int lanes, const int32_t* q_pos0, con
   if (lanes == 0 || max_n_q == 0 || n_q_rows == 0) return KVQ_OK;
   if (!q_pos0 || !n_q || !q_offset || !n_k || !k_offset || !workspace || !d_status) return KVQ_ERR_INVALID_ARG;
   int rc;
-  if ((rc = check_rows(q_nope)) || (rc = check_rows(q_rope)) || (rc = check_out_rows(out, n_q_rows, num_heads))) return rc;
+  if ((rc = check_rows(q_nope, n_q_rows, num_heads)) || (rc = check_rows(q_rope, n_q_rows, num_heads)) ||
+      (rc = check_out_rows(out, n_q_rows, num_heads)))
+    return rc;
   if (n_k_rows == 0) return KVQ_ERR_INVALID_ARG;   // (a query attends its own position at least)
-  if ((rc = check_rows(k_nope)) || (rc = check_rows(k_rope)) || (rc = check_rows(v))) return rc;
+  if ((rc = check_rows(k_nope, n_k_rows, num_heads)) || (rc = check_rows(k_rope, n_k_rows, 1)) ||
+      (rc = check_rows(v, n_k_rows, num_heads)))
+    return rc;
   if (!mappable(q_nope, n_q_rows, num_heads) || !mappable(q_rope, n_q_rows, num_heads) ||
       !mappable(k_nope, n_k_rows, num_heads) || !mappable(k_rope, n_k_rows, 1) || !mappable(v, n_k_rows, num_heads))
     return KVQ_ERR_UNSUPPORTED;
@@ -414,12 +418,12 @@ int kvq_latent_prefill_attn(int num_heads, int lanes, const int32_t* q_pos0, con
   a.n_q_rows = n_q_rows;
   a.max_n_k = max_n_k;
   a.n_k_rows = n_k_rows;
-  a.qn = rows_view(q_nope);
-  a.qr = rows_view(q_rope);
-  a.kn = rows_view(k_nope);
-  a.kr = rows_view(k_rope);
-  a.v = rows_view(v);
-  a.out = rows_view(out);
+  a.qn = rows_view(q_nope, n_q_rows, num_heads);
+  a.qr = rows_view(q_rope, n_q_rows, num_heads);
+  a.kn = rows_view(k_nope, n_k_rows, num_heads);
+  a.kr = rows_view(k_rope, n_k_rows, 1);
+  a.v = rows_view(v, n_k_rows, num_heads);
+  a.out = rows_view(out, n_q_rows, num_heads);
   a.scale_log2 = sm_scale * LOG2E;
   a.ws = static_cast<float*>(workspace);
   a.status = d_status;

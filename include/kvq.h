@@ -313,7 +313,8 @@ int paged_decode_attn_noalloc(const kvq_geom* geom, int layer, const void* pool,
  * into a graph; nothing is allocated and nothing waits.  A workspace serves calls that run one after the
  * other; calls that may overlap on the GPU (other streams, graphs replayed side by side) need one
  * each.  Outputs overlap neither an input nor themselves (a zero stride between rows or heads of an
- * output is KVQ_ERR_INVALID_ARG); inputs may share rows or heads through zero strides.  sm_scale is
+ * output is KVQ_ERR_INVALID_ARG); inputs may share heads through a zero head_stride and, except in
+ * kvq_latent_prefill_attn, rows through a zero row_stride.  sm_scale is
  * finite and not negative.  A result depends on the arguments alone, bit for bit: no atomics take
  * part in a sum.
  * The kernels are launched programmatically and let the next one of the stream start early: a kernel that the
@@ -332,8 +333,9 @@ typedef struct {
 } kvq_latent_geom;
 
 /* bf16 rows of device memory, [row][head][dim] with the dims contiguous; strides in elements,
- * multiples of 8 (one head: head_stride unused); ptr 16-byte aligned.  The struct itself lies in
- * host memory and is read during the call. */
+ * multiples of 8; ptr 16-byte aligned.  A stride that steps nowhere is not used and may be anything:
+ * head_stride with one head (and of latent, rope and k_rope, which have no heads), row_stride with
+ * one row.  The struct itself lies in host memory and is read during the call. */
 typedef struct {
   void* ptr;
   int64_t row_stride;

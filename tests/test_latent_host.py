@@ -224,3 +224,33 @@ def test_prefill_workspace_for_the_most_serves_every_smaller_call(L):
                 assert size[at[:i] + (axis[j - 1],) + at[i + 1:]] <= here, (at, i)
     rows = {kvq.latent_prefill_workspace_bytes(2, 16, r, 256, 16000) for r in (1, 512, 4096, 2 ** 31 - 1)}
     assert len(rows) == 1
+
+
+def _prefill_short(L, **kw):
+    """Without a workspace: stopped by the check of its size, the last one."""
+    a = dict(heads=16, rows=8, krows=64, qn=_rows(4096, 2048, 128), qr=_rows(8192, 1024, 64), kn=_rows(4096, 2048, 128),
+             kr=_rows(8192, 64), v=_rows(4096, 2048, 128), out=_rows(16384, 2048, 128))
+    a.update(kw)
+    return L.kvq_latent_prefill_attn(a["heads"], 1, 1024, 1040, 1056, 4, a["rows"], 1072, 1088, 64, a["krows"], a["qn"],
+                                     a["qr"], a["kn"], a["kr"], a["v"], 0.07, 1536, 0, a["out"], 2048, None)
+
+
+def test_unused_strides_may_be_anything(L):
+    """Head strides of rows without heads or with one, and row strides of one row: a caller need not set them.  (Each call
+    is stopped by a later check.)"""
+    odd = 12345
+    big = dict(lanes=2 ** 31 - 1, most=2 ** 31 - 1)
+    g, one = kvq.latent_geom(kvq.LATENT_BF16, 2, 16), kvq.latent_geom(kvq.LATENT_BF16, 2, 1)
+    for fn in ("kvq_latent_append", "kvq_latent_read"):
+        assert _append(L, g, fn, lat=_rows(4096, 512, odd), rope=_rows(8192, 64, odd), **big) == kvq.ERR_UNSUPPORTED
+        assert _append(L, g, fn, rows=1, lat=_rows(4096, odd), rope=_rows(8192, odd), **big) == kvq.ERR_UNSUPPORTED
+    short = dict(ws_bytes=0)
+    assert _attn(L, one, ql=_rows(4096, 512, odd), qr=_rows(8192, 64, odd), out=_rows(16384, 512, odd), **short) == kvq.ERR_WORKSPACE_TOO_SMALL
+    assert _attn(L, g, rows=1, ql=_rows(4096, odd, 512), qr=_rows(8192, odd, 64), out=_rows(16384, odd, 512), **short) == kvq.ERR_WORKSPACE_TOO_SMALL
+    assert _prefill_short(L, kr=_rows(8192, 64, odd)) == kvq.ERR_WORKSPACE_TOO_SMALL
+    assert _prefill_short(L, heads=1, qn=_rows(4096, 128, odd), qr=_rows(8192, 64, odd), kn=_rows(4096, 128, odd), v=_rows(4096, 128, odd),
+                          out=_rows(16384, 128, odd)) == kvq.ERR_WORKSPACE_TOO_SMALL
+    assert _prefill_short(L, rows=1, krows=1, qn=_rows(4096, odd, 128), qr=_rows(8192, odd, 64), kn=_rows(4096, odd, 128), kr=_rows(8192, odd),
+                          v=_rows(4096, odd, 128), out=_rows(16384, odd, 128)) == kvq.ERR_WORKSPACE_TOO_SMALL
+    assert _attn(L, g, ql=_rows(4096, 8192, odd), **short) == kvq.ERR_ALIGNMENT
+    assert _attn(L, one, ql=_rows(4096, odd), **short) == kvq.ERR_ALIGNMENT
