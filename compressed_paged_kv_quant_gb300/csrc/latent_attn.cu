@@ -998,7 +998,7 @@ template <int FMT, int N>
 static int launch_la(const LatentAttnArgs& a, const LaGrid& g, cudaStream_t stream) {
   using C = LaCfg<FMT, N>;
   const int64_t blocks = (int64_t)g.T * (g.W > 0 ? g.W : a.c.lanes);
-  if (blocks > INT32_MAX || (int64_t)a.c.lanes * ((a.max_seq_len + P - 1) / P) > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  if (blocks > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(latent_attn_tc<FMT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return KVQ_ERR_CUDA;
   const int rc = latent_launch(latent_attn_tc<FMT, N>, dim3((unsigned)blocks), C::THREADS, C::SMEM, stream, a, g);

@@ -234,11 +234,29 @@ int check_rows(const kvq_rows* r, int rows, int heads) {
   return KVQ_OK;
 }
 
+// Do two of the rows [row][head] of `dims` elements share an element?  Rows (r, h) and (r + i, h + k) are |i R - k H| apart
+// (for strides of unlike sign it is the pair (r, h + k), (r + i, h)), so for each k the i nearest to k H / R decide.
+bool rows_overlap(const kvq_rows* r, int rows, int heads, int dims) {
+  using wide = __int128;
+  const wide R = r->row_stride < 0 ? -(wide)r->row_stride : r->row_stride,
+             H = r->head_stride < 0 ? -(wide)r->head_stride : r->head_stride;
+  if (rows <= 1) return heads > 1 && H < dims;
+  if (R < dims) return true;
+  if (heads <= 1) return false;
+  if (H < dims) return true;
+  if (R >= (heads - 1) * H + dims || H >= (rows - 1) * R + dims) return false;   // one within the gaps of the other
+  for (int k = 1; k < heads; k++) {
+    const wide i = k * H / R < rows - 1 ? k * H / R : rows - 1, far = k * H - i * R;
+    if (far < dims || (i + 1 < rows && R - far < dims)) return true;
+  }
+  return false;
+}
+
 // rows that are written: no two at one place
-int check_out_rows(const kvq_rows* r, int rows, int heads) {
+int check_out_rows(const kvq_rows* r, int rows, int heads, int dims) {
   const int rc = check_rows(r, rows, heads);
   if (rc) return rc;
-  return (rows > 1 && r->row_stride == 0) || (heads > 1 && r->head_stride == 0) ? KVQ_ERR_INVALID_ARG : KVQ_OK;
+  return rows_overlap(r, rows, heads, dims) ? KVQ_ERR_INVALID_ARG : KVQ_OK;
 }
 
 // rows that tensor maps describe: strides that go forward, below 2^40 bytes (0: heads that share the rows)
@@ -287,8 +305,8 @@ int latent_tokens(bool append, const kvq_latent_geom* g, int layer, const void* 
   if (!pool || !page_table || !start_pos || !n_tok || !tok_offset || !d_status) return KVQ_ERR_INVALID_ARG;
   if (pool_bytes < latent_page_bytes(g)) return KVQ_ERR_INVALID_ARG;
   if (n_rows > 0) {
-    rc = append ? check_rows(latent, n_rows, 1) : check_out_rows(latent, n_rows, 1);
-    if (!rc) rc = append ? check_rows(rope, n_rows, 1) : check_out_rows(rope, n_rows, 1);
+    rc = append ? check_rows(latent, n_rows, 1) : check_out_rows(latent, n_rows, 1, LAT);
+    if (!rc) rc = append ? check_rows(rope, n_rows, 1) : check_out_rows(rope, n_rows, 1, LROPE);
     if (rc) return rc;
   }
   if (!latent || !rope) return KVQ_ERR_INVALID_ARG;
@@ -354,12 +372,13 @@ int kvq_paged_latent_attn(const kvq_latent_geom* g, int layer, const void* pool,
   if ((int64_t)max_seq_len > (int64_t)max_pages * P) return KVQ_ERR_INVALID_ARG;
   if (!(sm_scale >= 0.0f && sm_scale <= 1.0e38f)) return KVQ_ERR_INVALID_ARG;
   if ((int64_t)g->num_q_heads * max_n_q > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  if ((int64_t)lanes * (((int64_t)max_seq_len + P - 1) / P) > INT32_MAX) return KVQ_ERR_UNSUPPORTED;   // the page list
   if (lanes == 0 || max_n_q == 0 || n_q_rows == 0) return KVQ_OK;
   if (!pool || !page_table || !q_pos0 || !n_q || !q_offset || !seq_len || !workspace || !d_status)
     return KVQ_ERR_INVALID_ARG;
   if (pool_bytes < latent_page_bytes(g)) return KVQ_ERR_INVALID_ARG;
   if ((rc = check_rows(q_latent, n_q_rows, g->num_q_heads)) || (rc = check_rows(q_rope, n_q_rows, g->num_q_heads)) ||
-      (rc = check_out_rows(out, n_q_rows, g->num_q_heads)))
+      (rc = check_out_rows(out, n_q_rows, g->num_q_heads, LAT)))
     return rc;
   if (!aligned16(pool) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
   if (ws_bytes < latent_attn_needs(g->num_q_heads, lanes, max_n_q, max_seq_len)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
@@ -395,7 +414,7 @@ int kvq_latent_prefill_attn(int num_heads, int lanes, const int32_t* q_pos0, con
   if (!q_pos0 || !n_q || !q_offset || !n_k || !k_offset || !workspace || !d_status) return KVQ_ERR_INVALID_ARG;
   int rc;
   if ((rc = check_rows(q_nope, n_q_rows, num_heads)) || (rc = check_rows(q_rope, n_q_rows, num_heads)) ||
-      (rc = check_out_rows(out, n_q_rows, num_heads)))
+      (rc = check_out_rows(out, n_q_rows, num_heads, VDIM)))
     return rc;
   if (n_k_rows == 0) return KVQ_ERR_INVALID_ARG;   // (a query attends its own position at least)
   if ((rc = check_rows(k_nope, n_k_rows, num_heads)) || (rc = check_rows(k_rope, n_k_rows, 1)) ||

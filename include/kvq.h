@@ -312,8 +312,8 @@ int paged_decode_attn_noalloc(const kvq_geom* geom, int layer, const void* pool,
  * Every call: the device that owns the buffers is current; the launches go to `stream` and can be captured
  * into a graph; nothing is allocated and nothing waits.  A workspace serves calls that run one after the
  * other; calls that may overlap on the GPU (other streams, graphs replayed side by side) need one
- * each.  Outputs overlap neither an input nor themselves (a zero stride between rows or heads of an
- * output is KVQ_ERR_INVALID_ARG); inputs may share heads through a zero head_stride and, except in
+ * each.  Outputs overlap neither an input nor themselves (strides with which two rows or heads of an
+ * output share an element are KVQ_ERR_INVALID_ARG); inputs may share heads through a zero head_stride and, except in
  * kvq_latent_prefill_attn, rows through a zero row_stride.  sm_scale is
  * finite and not negative.  A result depends on the arguments alone, bit for bit: no atomics take
  * part in a sum.

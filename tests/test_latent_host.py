@@ -254,3 +254,35 @@ def test_unused_strides_may_be_anything(L):
                           v=_rows(4096, odd, 128), out=_rows(16384, odd, 128)) == kvq.ERR_WORKSPACE_TOO_SMALL
     assert _attn(L, g, ql=_rows(4096, 8192, odd), **short) == kvq.ERR_ALIGNMENT
     assert _attn(L, one, ql=_rows(4096, odd), **short) == kvq.ERR_ALIGNMENT
+
+
+def _shared(row, head, rows, heads, dims):
+    """By definition: does any element belong to two rows?"""
+    at = [r * row + h * head for r in range(rows) for h in range(heads)]
+    at.sort()
+    return any(b - a < dims for a, b in zip(at, at[1:]))
+
+
+def test_outputs_that_overlap_in_part_are_refused(L):
+    """Every layout of rows and heads whose elements meet, and no other (the accepted ones are stopped by the check of the
+    workspace, or of the grid)."""
+    g = kvq.latent_geom(kvq.LATENT_BF16, 2, 16)
+    three = kvq.latent_geom(kvq.LATENT_BF16, 2, 3)
+    seen = set()
+    for row in (8, 256, 504, 512, 520, 1016, 1024, 1032, 1536, 2048, 3080, 4096, 7680, 8192, -512, -1024, -8192, 1 << 40, 1 << 62):
+        for head in (8, 504, 512, 520, 1024, 1536, 1544, 2048, 4096, 8192, 16384, -512, -1032, -4096, -8192, 1 << 40, 1 << 62):
+            for geom, heads in ((g, 16), (three, 3)):
+                for rows in (1, 2, 3, 8):
+                    want = _shared(row, head, rows, heads, 512)
+                    got = _attn(L, geom, rows=rows, out=_rows(16384, row, head), ws_bytes=0)
+                    assert got == (kvq.ERR_INVALID_ARG if want else kvq.ERR_WORKSPACE_TOO_SMALL), (row, head, rows, heads)
+                    seen.add((want, rows > 1))
+    assert len(seen) == 4
+    for row, head in ((8, 128), (120, 128 * 8), (2048, 120), (128 * 3, 128), (256, 128)):
+        assert _prefill_short(L, out=_rows(16384, row, head)) == kvq.ERR_INVALID_ARG, (row, head)
+    for row, head in ((128, 128 * 8), (2048, 128), (2176, 136)):
+        assert _prefill_short(L, out=_rows(16384, row, head)) == kvq.ERR_WORKSPACE_TOO_SMALL, (row, head)
+    big = dict(lanes=2 ** 31 - 1, most=2 ** 31 - 1)
+    for lat, rope, rc in ((504, 64, kvq.ERR_INVALID_ARG), (512, 56, kvq.ERR_INVALID_ARG), (-504, 64, kvq.ERR_INVALID_ARG),
+                          (512, 64, kvq.ERR_UNSUPPORTED), (-512, -64, kvq.ERR_UNSUPPORTED), (576, 576, kvq.ERR_UNSUPPORTED)):
+        assert _append(L, g, "kvq_latent_read", lat=_rows(4096, lat), rope=_rows(8192, rope), **big) == rc, (lat, rope)
