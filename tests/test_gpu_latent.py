@@ -882,3 +882,41 @@ def test_expanded_parts_stay_in_their_workspace(kvq, heads, nqs, prefix):
     c.call()
     assert c.status.item() == 0 and bool((whole[size:] == 0xEE).all())
     c.check()
+
+
+@FORMATS
+@pytest.mark.parametrize("value", [3, -1])
+def test_lanes_beside_a_refused_count_are_answered(kvq, fmt, value):
+    """A lane with a bad count of queries is skipped: the other lanes are answered and its own rows left as they were."""
+    for lens in ([100, 200, 300, 64], [100, 900, 3000, 64]):
+        c = Absorbed(kvq, fmt, 16, lens, [1, 2, 1, 1], 270)
+        c.n_q[1] = value
+        c.call()
+        assert c.status.item() == kvq.STATUS_BAD_LEN
+        c.check(skip=(1,))
+
+
+@FORMATS
+@pytest.mark.parametrize("heads,lens,nqs", [(128, [1500, 700], [30, 1]), (128, [1500, 700], [40, 1]), (128, [2000, 5], [38, 3]),
+                                            (128, [700, 1300, 90], [12, 26, 2]), (100, [3000], [33]), (16, [1400, 600], [120, 304]),
+                                            (24, [900, 2500, 1], [70, 11, 1]), (128, [2600, 90], [10, 2]), (128, [1700], [25])])
+def test_chunks_of_many_row_tiles(kvq, fmt, heads, lens, nqs):
+    """Chunks whose rows take 20 to 80 tiles: few ranges of the page list (7, 5, 3 or 2) with a merge, and, above 76 tiles,
+    long lanes in one piece."""
+    c = Absorbed(kvq, fmt, heads, lens, nqs, 280 + heads, head_first=False)
+    c.call()
+    assert c.status.item() == 0
+    c.check()
+
+
+@FORMATS
+def test_inputs_that_share_rows_or_heads(kvq, fmt):
+    """Queries, latents and rotary keys broadcast through zero strides."""
+    c = Absorbed(kvq, fmt, 16, [700, 90], [3, 1], 290, head_first=False)
+    c.ql = c.ql[:1].contiguous().expand(c.rows, -1, -1)
+    c.qr = c.qr[:, :1].contiguous().expand(-1, 16, -1)
+    c.lat, c.rope = c.lat[:1].expand(790, -1), c.rope[5:6].expand(790, -1)
+    kvq.latent_append(c.g, c.layer, c.pool, c.dtable, i32([0, 0]), c.seq_len, i32([0, 700]), 700, c.lat, c.rope, c.status)
+    c.call()
+    assert c.status.item() == 0
+    c.check()
