@@ -4,8 +4,8 @@
 //   out[row][h] = sum_t softmax_t(scale (q_c . c_t + q_r . r_t)) c_t,  c 512 dims, r 64 dims
 //
 // One latent serves every head, so a token's 1,152 (bf16) or 656 (MXFP8) bytes feed
-// 2 * 1,088 * heads FLOP: with up to 64 rows (query, head) in a CTA the bound is HBM, with 128
-// heads it is the rate at which shared memory feeds the tensor cores.
+// 2 * 1,088 * heads FLOP: with 16 rows (query, head) in a CTA the bound is HBM, with 64 it is the rate at
+// which shared memory feeds the tensor cores, with 32 it is near both.
 //
 // Tile: 64 keys (a page) x N rows (16, 32 or 64; row = query * heads + head), transposed:
 //   S^T [64 keys][N]   = K . Q^T   M = 64, K = 576: A = the page as it lies (K-major, swizzled)
@@ -21,7 +21,9 @@
 // Softmax: a row's scores are taken relative to a reference that follows the row's maximum.  It moves only when
 // a score passes it by more than 2^8 (and with a part's first keys), which one barrier with a vote
 // detects; the maxima are reduced, and O is rescaled, only then.  l is summed in FP32 from the unrounded weights,
-// P goes to the tensor cores in bf16 (the type of V).
+// P goes to the tensor cores in bf16 (the type of V): half a bf16 step a weight, as much as the output's own rounding
+// (with it the error against 64 bits is 1.7e-3 to 2.1e-3 of the output's norm, 1.7e-3 of which a P in 32 bits has too).  P as
+// two bf16 terms would double the products of P.V.
 //
 // Work: the (lane, page) list is cut into W equal ranges, one CTA a range and row tile, so ragged
 // lanes balance; a lane within one range is finished there, else its parts are FP32 partials that
@@ -31,7 +33,7 @@
 // Every wait is bounded; on a timeout the CTA flags KVQ_STATUS_TIMEOUT and ends.
 //
 // Measured, whole calls: 8 lanes x 40,960 tokens, bf16, 16 heads 70 us (5.4 TB/s, 80% of the copy bandwidth: HBM
-// bound), 64 heads 84, 128 heads 112 (815 TFLOP/s).  With 64 rows a page takes 2,570 clocks: the tensor cores read 147 KB
+// bound), 32 heads 75, 64 heads 84, 128 heads 112 (815 TFLOP/s).  With 64 rows a page takes 2,570 clocks: the tensor cores read 147 KB
 // for the scores and 98 for P.V, the page's copy writes 74, all through shared memory at 128 B a clock.  MXFP8, 16
 // heads 58 us (1.2 us a page; 236 KB through shared memory, and the conversion's latencies), 128 heads 131.  One lane
 // of 257 tokens 12.4 us, latencies of five pages one after another.

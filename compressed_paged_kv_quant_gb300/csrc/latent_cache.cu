@@ -10,7 +10,7 @@
 // A warp takes one token; lane l holds dims 16l .. 16l + 15 (32 contiguous bytes), so a group's
 // maximum is one shuffle away and a lane's codes are one 16 B store.  Both kernels are bound by
 // HBM (1,152 + 1,152 or 656 B a token).  Measured: append of 65,536 tokens to MXFP8 20 us (5.9 TB/s), read of
-// 307,000 tokens from MXFP8 86 us (6.2 TB/s, 91% of the copy bandwidth), a step of 32 tokens 3 us (launch).
+// 307,000 tokens from MXFP8 86 us (6.2 TB/s, 91% of the copy bandwidth), a step of 32 tokens 2 us (launch).
 #include "latent.cuh"
 
 namespace kvq {

@@ -14,10 +14,13 @@
 // A box may run past the keys that the lane's queries attend, into rows of another lane: the softmax masks the
 // scores and, in the lane's last tile, writes zeros over those value rows before their products.
 // The softmax's reference maximum moves only when a row's maximum passes it by more than 2^8; l is
-// summed in FP32 from the unrounded weights, P is bf16 (the type of V).
+// summed in FP32 from the unrounded weights, P is bf16 (the type of V): half a bf16 step a weight, as much as the
+// output's own rounding (with it the error against 64 bits is 1.8e-3 to 2.3e-3 of the output's norm, 1.5e-3 to 1.7e-3 of which
+// a P in 32 bits has too).  P as two bf16 terms would double the products of P.V.
 // Few rows over long keys are split along the keys: FP32 partials, merged by latent_prefill_combine.
-// Measured: 4,096 x 128 heads 480 us (1.43 PFLOP/s, 75% of the matrix-product rate; 505 us back to back for seconds,
-// under the power limit), 1,024 x 32 heads after 15,000 tokens 211 us (1.54 PFLOP/s).  While a CTA's tiles run
+// Measured, inputs changing from call to call: 4,096 x 128 heads 515 us (1.33 PFLOP/s, 70% of the matrix-product rate),
+// 1,024 x 32 heads after 15,000 tokens 229 us (1.42 PFLOP/s).  With the same inputs again and again 480 to 500 (the power
+// limit decides) and 214.  While a CTA's tiles run
 // the tensor pipe is full; the rest is a CTA's start (2.5 us until the first 224 KB have come), its first
 // softmax and its end.
 // Every wait is bounded; on a timeout the CTA flags KVQ_STATUS_TIMEOUT and ends.
